@@ -28,11 +28,6 @@ namespace {
 constexpr int64_t SEL_WARP_MAX = 1024;     // longest row of the one-warp kernels
 constexpr int64_t SEL_CTA_MAX = 32768;     // longest row of the one-CTA kernels
 
-// The score of a key.
-__device__ __forceinline__ float sel_value(uint32_t key) {
-    return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
-}
-
 // ------------------------------------------------------- one warp a row --
 template <int I>
 __global__ void __launch_bounds__(256)
@@ -1407,20 +1402,6 @@ __global__ void __launch_bounds__(256) select_sample_kernel(SelLong L) {
     }
 }
 
-// A range of keys as bounds of scores: of a score f, f >= lo says that its key is in
-// the range or above, f > hi that it is above (a range that takes in NaN, the key 0,
-// says so: its passes compare keys).
-struct SelRange {
-    float lo, hi;
-    bool nan;
-    __device__ __forceinline__ SelRange(uint32_t first, uint32_t span) {
-        constexpr uint32_t MINUS_INF = 0x007fffffu;
-        nan = first == 0u;
-        lo = first <= MINUS_INF ? -CUDART_INF_F : sel_value(first);
-        hi = first + span < MINUS_INF ? -CUDART_INF_F : sel_value(first + span);   // beyond +inf: a NaN, nothing is above
-    }
-};
-
 // body(score, place, real) for the scores of a chunk [a, b) that thread t sees: places
 // a + j SEL_T + t, SEL_I loads in flight.
 template <typename Body>
@@ -1516,11 +1497,11 @@ __global__ void __launch_bounds__(SEL_T, 3) select_hist_kernel(SelLong L, int pa
     }
 }
 
-// One block finds A among the at most SEL_TIE keys of the range, and every chunk's
-// counts, by reading the row twice.
+// One block finds A among the at most SEL_TIE keys of the range (what the last pass
+// leaves), and every chunk's counts, by reading the row twice.
 constexpr int SEL_TIE = 1 << (32 - 2 * SEL_BITS);
 __device__ void select_alone(const SelLong &L, SelRow *R, const float *r, uint32_t *cnt, uint32_t *s_tie) {
-    const uint32_t lo = R->lo, span = R->span;
+    const uint32_t lo = R->lo, span = min(R->span, (uint32_t)SEL_TIE - 1u);   // (no more than s_tie holds, whatever is there)
     for (int i = threadIdx.x; i < SEL_TIE; i += SEL_T) s_tie[i] = 0u;
     __syncthreads();
     for (int64_t i = threadIdx.x; i < L.n; i += SEL_T) {

@@ -5,16 +5,9 @@
 #include <cuda_fp16.h>
 
 #include "lapsum_device.cuh"
+#include "select_keys.cuh"
 
 namespace lapsum {
-
-// Order-preserving key of the selection, ASCENDING with the score: -0 and +0
-// share a key, a NaN gets 0, below -inf (0x007fffff).
-__device__ __forceinline__ uint32_t sel_key(float f) {
-    const uint32_t u = __float_as_uint(f + 0.0f);   // -0 + 0 = +0
-    const uint32_t k = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return f != f ? 0u : k;
-}
 
 __device__ __forceinline__ unsigned lanes_below(int lane) { return (1u << lane) - 1u; }
 

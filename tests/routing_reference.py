@@ -70,3 +70,34 @@ def half_step(dtype):
     import torch
     f = torch.finfo(dtype)
     return f.eps / 2, f.smallest_normal * f.eps / 2
+
+
+ABOUT_ZERO = ["zeros and subnormals", "mostly subnormals", "deep", "both signs", "normals below", "zeros alone"]
+
+
+def about_zero(kind, n, k, seed=0):
+    """A row of zeros of both signs and subnormals: the keys just below zero's.  k - k / 16 of its
+    scores (deep: two thirds of k) are zero or more, so that the k-th largest is a negative subnormal."""
+    g = np.random.default_rng(seed + n + k)
+    tiny = 2.0 ** -149
+    top = max(k - max(k // (3 if kind == "deep" else 16), 1), 1)
+    r = np.empty(n)
+    place = g.permutation(n)
+    zero, rest = place[:top], place[top:]
+    r[zero] = np.where(g.random(zero.size) < 0.5, 0.0, -0.0)
+    if kind == "zeros and subnormals":           # few subnormals, then ordinary scores far below
+        r[rest] = -1.0 - g.random(rest.size)
+        some = rest[:k - top + (n - k) // 4 + 1]
+        r[some] = -tiny * g.integers(1, 1 << 21, some.size)
+    elif kind == "mostly subnormals":
+        r[rest] = -tiny * g.integers(1, 1 << 23, rest.size)
+    elif kind == "deep":
+        r[rest] = -tiny * g.integers(1, 4096, rest.size)
+    elif kind == "both signs":
+        r[zero] = np.where(g.random(zero.size) < 0.5, r[zero], tiny * g.integers(1, 4096, zero.size))
+        r[rest] = -tiny * g.integers(1, 4096, rest.size)
+    elif kind == "normals below":                # the last subnormals, and normals about the smallest
+        r[rest] = -tiny * g.integers((1 << 23) - 2048, (1 << 23) + 2048, rest.size)
+    else:
+        r[rest] = np.where(g.random(rest.size) < 0.5, 0.0, -0.0)
+    return r.astype(np.float32)
