@@ -1729,7 +1729,14 @@ bool sel_sizes_ok(int64_t rows, int64_t n, int64_t k) {
 }
 
 // ---------------------------------------------------------- the gradient --
-// A shifted pair of sums: sum e and sum dw e with e = 2^{m - |x|}.
+// The smaller one; a NaN, where one is (fminf drops it).
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float m;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+// A shifted pair of sums: sum e and sum dw e with e = 2^{m - |x|}.  A NaN score or
+// threshold stays in m, and so makes both sums and the row's whole gradient NaN.
 struct GradAcc {
     float m;
     double sf, sg;
@@ -1737,7 +1744,7 @@ struct GradAcc {
 __device__ __forceinline__ GradAcc ga_merge(GradAcc a, GradAcc b) {
     if (b.m == CUDART_INF_F) return a;
     if (a.m == CUDART_INF_F) return b;
-    const float m = fminf(a.m, b.m);
+    const float m = min_nan(a.m, b.m);
     const double fa = (double)exp2f(m - a.m), fb = (double)exp2f(m - b.m);
     return {m, a.sf * fa + b.sf * fb, a.sg * fa + b.sg * fb};
 }
@@ -1751,7 +1758,7 @@ __device__ __forceinline__ GradAcc ga_warp(GradAcc a) {
     return a;
 }
 __device__ __forceinline__ float ax_of(const XForm &xf, float r) {
-    return fminf(fabsf(xf(r)), 3.0e38f);   // |x| may overflow fp32 (t tiny): keep the shift finite
+    return min_nan(fabsf(xf(r)), 3.0e38f);   // |x| may overflow fp32 (t tiny): keep the shift finite
 }
 
 struct GradRow {
@@ -1795,14 +1802,14 @@ select_grad_kernel(const float *__restrict__ scores, const double *__restrict__ 
     for (int j = 0; j < I; ++j) {
         const int i = j * T + tid;
         ax[j] = i < n ? ax_of(xf, r[i]) : CUDART_INF_F;
-        m = fminf(m, ax[j]);
+        m = min_nan(m, ax[j]);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fminf(m, __shfl_xor_sync(FULL, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = min_nan(m, __shfl_xor_sync(FULL, m, o));
     if (T > 32) {
         if (lane == 0) s_m[warp] = m;
         __syncthreads();
-        for (int w = 0; w < NW; ++w) m = fminf(m, s_m[w]);
+        for (int w = 0; w < NW; ++w) m = min_nan(m, s_m[w]);
     }
     GradAcc a{m, 0.0, 0.0};
     float sf = 0.f;
@@ -1913,10 +1920,10 @@ select_grad_ring_kernel(const float *__restrict__ scores, const double *__restri
         auto add = [&](const float (&ax)[8]) {
             float lm = ax[0];
 #pragma unroll
-            for (int i = 1; i < 8; ++i) lm = fminf(lm, ax[i]);
-            if (lm < m) {
+            for (int i = 1; i < 8; ++i) lm = min_nan(lm, ax[i]);
+            if (!(lm >= m)) {              // (once NaN: m stays it)
                 sf *= m == CUDART_INF_F ? 0.0 : (double)exp2f(lm - m);
-                m = lm;
+                m = min_nan(m, lm);
             }
             float s = 0.f;
 #pragma unroll
@@ -1954,7 +1961,7 @@ select_grad_ring_kernel(const float *__restrict__ scores, const double *__restri
         // the smallest |x| of the row
         float wm = m;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) wm = fminf(wm, __shfl_xor_sync(FULL, wm, o));
+        for (int o = 16; o > 0; o >>= 1) wm = min_nan(wm, __shfl_xor_sync(FULL, wm, o));
         const bool warp_bad = __any_sync(FULL, !ok);
         if (lane == 0) {
             S.m[warp] = wm;
@@ -1965,7 +1972,7 @@ select_grad_ring_kernel(const float *__restrict__ scores, const double *__restri
         int gave_up = S.bad[0];
 #pragma unroll
         for (int w = 1; w < G; ++w) {
-            lo = fminf(lo, S.m[w]);
+            lo = min_nan(lo, S.m[w]);
             gave_up |= S.bad[w];
         }
         if (gave_up) {                     // this row and the later ones from memory
@@ -1979,11 +1986,11 @@ select_grad_ring_kernel(const float *__restrict__ scores, const double *__restri
             }
             lo = m;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) lo = fminf(lo, __shfl_xor_sync(FULL, lo, o));
+            for (int o = 16; o > 0; o >>= 1) lo = min_nan(lo, __shfl_xor_sync(FULL, lo, o));
             M.sync();
             if (lane == 0) S.m[warp] = lo;
             M.sync();
-            for (int w = 0; w < G; ++w) lo = fminf(lo, S.m[w]);
+            for (int w = 0; w < G; ++w) lo = min_nan(lo, S.m[w]);
         }
         sf = m == CUDART_INF_F ? 0.0 : sf * (double)exp2f(lo - m);
         // the selected scores' part, out of the ring
@@ -2131,10 +2138,10 @@ __global__ void __launch_bounds__(GL_T) select_grad_sum_kernel(GradLong L) {
         for (int q = 0; q < 8; ++q) {
             const int64_t i = i0 + q * GL_T + threadIdx.x;
             ax[q] = i < a1 ? ax_of(xf, r[i]) : CUDART_INF_F;
-            m = fminf(m, ax[q]);
+            m = min_nan(m, ax[q]);
         }
         if (m == CUDART_INF_F) continue;
-        if (m < acc.m) {
+        if (!(m >= acc.m)) {
             if (acc.m != CUDART_INF_F) acc.sf *= (double)exp2f(m - acc.m);
             acc.m = m;
         }

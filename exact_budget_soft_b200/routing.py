@@ -117,7 +117,7 @@ def select_backward(scores: torch.Tensor, b: torch.Tensor, idx: torch.Tensor, dw
                     grad_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The gradient of the soft gate when only its selected prices were used: ``backward``
     for an upstream gradient that is dw at idx (as ``select`` returns it) and zero elsewhere.
-    A row whose indices do not ascend within [0, n) gets NaN."""
+    A row whose indices do not ascend within [0, n), or with a NaN score or threshold, gets NaN."""
     L._need(scores, "scores")
     rows, n = L._as_rows(scores)
     dev = scores.device

@@ -436,7 +436,8 @@ LAPSUM_API int lapsum_select(const float *scores_dev, const float *p_dev, int64_
  * scores: g[idx[j]] = dw[j] (dw_dev fp32 [rows][k], idx_dev as lapsum_select
  * returns it).  grad_out_dev fp32 [rows][n], every value written; it may not
  * alias an input.  A row whose indices are not strictly ascending within
- * [0, n) gets NaN in every grad.  Temperatures as for lapsum_backward.
+ * [0, n), or with a NaN among its scores or as its threshold, gets NaN in every
+ * grad.  Temperatures as for lapsum_backward.
  */
 LAPSUM_API int64_t lapsum_select_backward_scratch(int64_t rows, int64_t n);     /* bytes; LAPSUM_ERR_ARG */
 LAPSUM_API int lapsum_select_backward(const float *scores_dev, const double *b_dev, const int32_t *idx_dev,
