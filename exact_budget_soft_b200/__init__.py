@@ -79,7 +79,7 @@ EXPORTS = ["lapsum_forward", "lapsum_forward_ex", "lapsum_backward", "lapsum_get
            "lapsum_step_host", "lapsum_select_scratch", "lapsum_select", "lapsum_select_backward_scratch",
            "lapsum_select_backward", "lapsum_route_scratch", "lapsum_route_build", "lapsum_dispatch",
            "lapsum_dispatch_backward", "lapsum_combine", "lapsum_combine_backward", "lapsum_clip_scratch",
-           "lapsum_clip_grads"]
+           "lapsum_clip_grads", "lapsum_selftest_give_up"]
 SHARD_PART = 10   # doubles in a slice's streaming-pass record (LAPSUM_SHARD_PART)
 
 
@@ -134,6 +134,8 @@ def _load() -> C.CDLL:
     lib.lapsum_combine_backward.argtypes = [vp, vp, vp, C.c_int32, i64, rp, vp, vp, vp]
     lib.lapsum_clip_scratch.argtypes = [i64]
     lib.lapsum_clip_grads.argtypes = [i64, vp, vp, vp, dbl, vp, vp, vp, i64, vp]
+    lib.lapsum_selftest_give_up.argtypes = [C.c_int32, C.c_int32]
+    lib.lapsum_selftest_give_up.restype = C.c_int
     for name in ("lapsum_select_scratch", "lapsum_select_backward_scratch", "lapsum_route_scratch",
                  "lapsum_clip_scratch"):
         getattr(lib, name).restype = C.c_int64
@@ -300,6 +302,12 @@ def selftest_math(which: int, x: torch.Tensor) -> tuple[torch.Tensor, torch.Tens
     _check(lib.lapsum_selftest_math(int(which), x.data_ptr(), out.data_ptr(), ref.data_ptr(), x.numel(),
                                     _stream(None)), "lapsum_selftest_math")
     return out, ref
+
+
+def selftest_give_up(wait: int, row: int | None):
+    """Checked build: the waits of a kind (0 reads, 1 the writing warp's) report that they gave
+    up from a block's row-th row on; None: as they are."""
+    _check(lib.lapsum_selftest_give_up(int(wait), 2 ** 31 - 1 if row is None else int(row)), "lapsum_selftest_give_up")
 
 
 def profile_read() -> dict:

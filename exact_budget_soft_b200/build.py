@@ -14,7 +14,7 @@ LIB_CHECKED = os.path.join(HERE, "liblapsum_checked.so")
 SOURCES = ["lapsum_api.cu", "k_rows.cu", "k_bracket.cu", "k_radix.cu", "k_band.cu", "k_noalloc.cu", "k_shard.cu",
            "k_select.cu", "k_route.cu", "k_tokens.cu", "k_clip.cu"]
 HEADERS = ["lapsum_internal.h", "lapsum_kernels.h", "lapsum_device.cuh", "scan_solve.cuh",
-           "lapsum_launch.h", "route_common.cuh", "select_keys.cuh"]
+           "lapsum_launch.h", "route_common.cuh", "select_keys.cuh", "give_up.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",

@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "give_up.cuh"
 #include "lapsum_kernels.h"
 #include "lapsum_launch.h"
 #include "route_common.cuh"
@@ -698,7 +699,7 @@ select_row_kernel(const float *__restrict__ scores, const float *__restrict__ p,
             M.sync();
             const uint32_t bound = S.bound;
             Kept<G> kept(S, M, bound);
-            bool ok = warp_wait(&All.turn[M.id], turn & 1u);
+            bool ok = waited(warp_wait(&All.turn[M.id], turn & 1u), GIVE_UP_READ, (int)turn);
             ++turn;
             kept.ends(r, n, head, body);
             for (int a = 0; a < body && ok; a += RS_CHUNK) {
@@ -820,7 +821,7 @@ select_wide_kernel(const float *__restrict__ scores, const float *__restrict__ p
         int i = 0;
         for (int row = blockIdx.x; row < rows; row += gridDim.x, ++i) {
             int32_t *idx = idx_out + (int64_t)row * k;
-            if (!warp_wait(&All.stage_full[i & 1], (i >> 1) & 1, 16)) {   // longer than the search's own waits can take
+            if (!waited(warp_wait(&All.stage_full[i & 1], (i >> 1) & 1, 16), GIVE_UP_WRITE, i)) {   // longer than the search's own waits can take
                 // never seen: two rows at most were handed over, and none of them is left stale
                 for (int z = 0; z < 2 && i + z < All.direct[(i + z) & 1] && row + z * (int)gridDim.x < rows; ++z)
                     for (int j = lane; j < k; j += 32) idx[(int64_t)z * gridDim.x * k + j] = -1;
@@ -854,7 +855,8 @@ select_wide_kernel(const float *__restrict__ scores, const float *__restrict__ p
             const float *r = scores + (int64_t)row * n;
             int head, body;
             rs_granules(r, n, head, body);
-            ok = ok && warp_wait(&All.bound_full[buf], (i >> 1) & 1) && warp_wait(&All.list_empty[buf], ((i >> 1) & 1) ^ 1);
+            ok = ok && waited(warp_wait(&All.bound_full[buf], (i >> 1) & 1), GIVE_UP_READ, i) &&
+                 warp_wait(&All.list_empty[buf], ((i >> 1) & 1) ^ 1);
             const uint32_t bound = All.bound[buf];
             const float lo = sel_value(bound);
             const float under = sel_under(lo);
@@ -1050,7 +1052,8 @@ select_held_kernel(const float *__restrict__ scores, const float *__restrict__ p
     };
     if (blockIdx.x < rows) fetch(blockIdx.x);
     uint32_t phase = 0;
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, phase ^= 1u) {
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, phase ^= 1u, ++turn) {
         int head, body;
         rs_granules(scores + row * n, n, head, body);
         const float *x = H.row + ((4 - head) & 3);
@@ -1058,7 +1061,7 @@ select_held_kernel(const float *__restrict__ scores, const float *__restrict__ p
             H.lo = 0xffffffffu;
             H.hi = 0xff800000u;            // +infinity
         }
-        const bool ok = !bulk || mbar_wait(&H.bar, phase, BULK_WAIT_CAP);
+        const bool ok = !bulk || waited(mbar_wait(&H.bar, phase, BULK_WAIT_CAP), GIVE_UP_READ, turn);
         if (!__syncthreads_and(ok)) {
             mbar_wait(&H.bar, phase, BULK_WAIT_CAP);   // (the copy may still land, with the same values)
             bulk = false;
@@ -1891,7 +1894,8 @@ select_grad_ring_kernel(const float *__restrict__ scores, const double *__restri
     M.id = 0;
     int slot0 = 0, phase0 = 0;             // of the row's first chunk
     bool ring = true;                      // false once a wait has given up: rows are then read from memory
-    for (int row = blockIdx.x; row < rows; row += gridDim.x) {
+    int turn = 0;
+    for (int row = blockIdx.x; row < rows; row += gridDim.x, ++turn) {
         const float *r = scores + (int64_t)row * n;
         const int32_t *idx = idx_in + (int64_t)row * k;
         const float *dw = dw_in + (int64_t)row * k;
@@ -1949,7 +1953,7 @@ select_grad_ring_kernel(const float *__restrict__ scores, const double *__restri
         bool ok = true;
         if (ring)                          // the whole row first: a wait that gives up is then known to all
             for (int a = 0; a < body; a += CHUNK) {
-                ok = ok && mbar_wait(&S.full[slot], phase, BULK_WAIT_CAP);
+                ok = ok && waited(mbar_wait(&S.full[slot], phase, BULK_WAIT_CAP), GIVE_UP_READ, turn);
                 if (ok) {
                     float ax[8];
                     eight(slot, a, ax);
@@ -1975,7 +1979,7 @@ select_grad_ring_kernel(const float *__restrict__ scores, const double *__restri
             lo = min_nan(lo, S.m[w]);
             gave_up |= S.bad[w];
         }
-        if (gave_up) {                     // this row and the later ones from memory
+        if (gave_up || !ring) {            // this row and the later ones from memory
             ring = false;
             m = edge_ax;
             sf = edge >= 0 ? 1.0 : 0.0;
@@ -2250,6 +2254,8 @@ cudaError_t run_grad(const float *s, const double *b, const int32_t *idx, const 
 }
 
 }  // namespace
+
+cudaError_t select_give_up(int kind, int turn) { return set_give_up((GiveUp)kind, turn); }
 }  // namespace lapsum
 
 using namespace lapsum;

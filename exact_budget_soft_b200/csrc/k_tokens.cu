@@ -25,6 +25,7 @@
 #include <initializer_list>
 #include <type_traits>
 
+#include "give_up.cuh"
 #include "lapsum_kernels.h"
 #include "lapsum_launch.h"
 #include "route_common.cuh"
@@ -365,16 +366,16 @@ to_tokens_ring_kernel(Rows R, int seg_bytes, int segs) {
     }
     // ---- the warps that add: vectors t + v TS_T of a segment (EVEN), or values t + j TS_T
     const int tid = threadIdx.x;
-    int stage = 0, phase = 0;
+    int stage = 0, phase = 0, turn = 0;
     bool ok = true;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x, ++turn) {
         const int64_t token = item / segs, off = item % segs * seg_bytes;
         const int len = (int)min((int64_t)seg_bytes, R.row_bytes - off);
         float acc[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) acc[i] = 0.f;
         for (bool last = false; !last;) {
-            ok = ok && mbar_wait(&S.full[stage], phase, BULK_WAIT_CAP);
+            ok = ok && waited(mbar_wait(&S.full[stage], phase, BULK_WAIT_CAP), GIVE_UP_READ, turn);
             if (!ok) break;
             const uint4 note = S.note[stage];
             const float w = __uint_as_float(note.z);
@@ -704,6 +705,8 @@ cudaError_t run_combine_grad(const Rows &A, int vb, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t tokens_give_up(int kind, int turn) { return set_give_up((GiveUp)kind, turn); }
 }  // namespace lapsum
 
 using namespace lapsum;

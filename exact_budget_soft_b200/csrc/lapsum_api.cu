@@ -826,6 +826,19 @@ int lapsum_selftest_math(int which, const double *in, double *out, double *ref, 
     return LAPSUM_OK;
 }
 
+int lapsum_selftest_give_up(int32_t wait, int32_t row) {
+#ifdef LAPSUM_CHECKED
+    if ((wait != LAPSUM_GIVE_UP_READ && wait != LAPSUM_GIVE_UP_WRITE) || row < 0) return LAPSUM_ERR_ARG;
+    LAPSUM_TRY(select_give_up(wait, row));
+    LAPSUM_TRY(tokens_give_up(wait, row));
+    return LAPSUM_OK;
+#else
+    (void)wait;
+    (void)row;
+    return LAPSUM_ERR_ARG;
+#endif
+}
+
 int lapsum_profile_read(const char **names, int64_t *launches, double *total_ms, int max) {
     cudaDeviceSynchronize();
     std::lock_guard<std::mutex> lk(g_prof_mu);

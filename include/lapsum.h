@@ -281,6 +281,16 @@ LAPSUM_API int lapsum_selftest_math(int which, const double *in_dev, double *out
                                     double *ref_dev, int64_t n, struct CUstream_st *stream);
 
 /*
+ * Self-test of the bounded waits, in the checked build (-DLAPSUM_CHECKED; else
+ * LAPSUM_ERR_ARG): from a block's row-th row on, waits of one kind in the routing
+ * kernels report that they gave up, though what they waited for has come.  The
+ * next call changes it; 2^31 - 1 ends it.  Synchronous, on the current device.
+ */
+#define LAPSUM_GIVE_UP_READ  0   /* the wait for a row that is copied into shared memory */
+#define LAPSUM_GIVE_UP_WRITE 1   /* the wait of the warp that writes a long row's selection */
+LAPSUM_API int lapsum_selftest_give_up(int32_t wait, int32_t row);
+
+/*
  * Backward without any device allocation.  The method's pages have no
  * counterpart of this entry point: it exists for callers that may not call
  * cudaMalloc while they run -- for instance a plugin inside a host framework

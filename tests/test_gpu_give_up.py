@@ -1,0 +1,61 @@
+"""What the routing kernels do when a bounded wait gives up.  The checked build has waits say
+so from a block's second row on, although the copies have landed (lapsum_selftest_give_up);
+rows are then read from memory, with the same results, or marked, and none is stale.
+
+Each case runs in a child process, as the checked build is loaded instead of the other."""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+HEAD = """
+import torch
+import exact_budget_soft_b200 as L
+from exact_budget_soft_b200 import routing as R
+assert L.CHECKED
+READ, WRITE = 0, 1
+torch.manual_seed(1)
+
+def given_up(wait, row, call):
+    want = call()
+    torch.cuda.synchronize()
+    L.selftest_give_up(wait, row)
+    got = call()
+    torch.cuda.synchronize()
+    L.selftest_give_up(wait, None)
+    again = call()
+    assert all(torch.equal(a, b) for a, b in zip(again, want))
+    return want, got
+"""
+
+
+def child(code, *values):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    r = subprocess.run([sys.executable, "-c", HEAD + code.format(*values) + "\nprint('as expected')\n"], cwd=ROOT,
+                       env=dict(os.environ, LAPSUM_CHECKED="1", PYTHONPATH=ROOT), capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "as expected" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+GRADIENT = """
+rows, n, k, row = {}, {}, {}, {}
+r = torch.randn(rows, n, device="cuda")
+idx, _ = R.select(r, k)
+dw = torch.randn(rows, k, device="cuda")
+b = torch.full((rows,), 1.3, dtype=torch.float64, device="cuda")
+want, got = given_up(READ, row, lambda: (R.select_backward(r, b, idx, dw, 0.1),))
+off = (want[0] != got[0]).any(dim=1).nonzero().flatten().tolist()
+assert not off, (len(off), off[:5])
+"""
+
+
+@pytest.mark.parametrize("rows,n,k", [(9000, 1501, 30), (5000, 4000, 200), (2500, 8190, 3), (1000, 12_003, 600), (600, 30_001, 99)])
+@pytest.mark.parametrize("row", [0, 1])
+def test_the_gradient_goes_on_from_memory(rows, n, k, row):
+    child(GRADIENT, rows, n, k, row)

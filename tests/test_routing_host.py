@@ -145,3 +145,10 @@ def test_python_refusals_name_the_argument():
 def test_exports_cover_the_routing_calls():
     for name in ("lapsum_select", "lapsum_route_build", "lapsum_dispatch", "lapsum_combine", "lapsum_clip_grads"):
         assert name in L.EXPORTS and getattr(L.lib, name)
+
+
+def test_waits_give_up_on_request_in_the_checked_build_alone():
+    if not L.CHECKED:
+        assert L.lib.lapsum_selftest_give_up(0, 1) == L.ERR_ARG
+    for wait, row in ((2, 0), (-1, 0), (0, -1)):
+        assert L.lib.lapsum_selftest_give_up(wait, row) == L.ERR_ARG
