@@ -855,8 +855,10 @@ select_wide_kernel(const float *__restrict__ scores, const float *__restrict__ p
             const float *r = scores + (int64_t)row * n;
             int head, body;
             rs_granules(r, n, head, body);
-            ok = ok && waited(warp_wait(&All.bound_full[buf], (i >> 1) & 1), GIVE_UP_READ, i) &&
-                 warp_wait(&All.list_empty[buf], ((i >> 1) & 1) ^ 1);
+            // a search that still reads these lists' counts must not see them change: without
+            // room this warp ends, and the searches' waits for it run out
+            if (!warp_wait(&All.list_empty[buf], ((i >> 1) & 1) ^ 1)) return;
+            ok = ok && waited(warp_wait(&All.bound_full[buf], (i >> 1) & 1), GIVE_UP_READ, i);
             const uint32_t bound = All.bound[buf];
             const float lo = sel_value(bound);
             const float under = sel_under(lo);

@@ -43,6 +43,23 @@ def child(code, *values):
     assert r.returncode == 0 and "as expected" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
 
 
+SELECTION = """
+rows, n, k, row = {}, {}, {}, {}
+r = torch.randn(rows, n, device="cuda")
+p = torch.rand(rows, n, device="cuda")
+want, got = given_up(READ, row, lambda: R.select(r, k, p))
+assert torch.equal(want[0].long(), torch.topk(r, k).indices.sort(dim=1).values)
+assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+"""
+
+
+@pytest.mark.parametrize("rows,n,k", [(9000, 1501, 9), (100, 3000, 30), (3000, 7000, 40), (1500, 12_003, 100), (700, 30_001, 200),
+                                      (400, 20_000, 1500)])
+@pytest.mark.parametrize("row", [0, 1])
+def test_the_selection_goes_on_from_memory(rows, n, k, row):
+    child(SELECTION, rows, n, k, row)
+
+
 GRADIENT = """
 rows, n, k, row = {}, {}, {}, {}
 r = torch.randn(rows, n, device="cuda")
