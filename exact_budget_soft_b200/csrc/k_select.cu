@@ -824,7 +824,10 @@ select_wide_kernel(const float *__restrict__ scores, const float *__restrict__ p
             if (!waited(warp_wait(&All.stage_full[i & 1], (i >> 1) & 1, 16), GIVE_UP_WRITE, i)) {   // longer than the search's own waits can take
                 // never seen: two rows at most were handed over, and none of them is left stale
                 for (int z = 0; z < 2 && i + z < All.direct[(i + z) & 1] && row + z * (int)gridDim.x < rows; ++z)
-                    for (int j = lane; j < k; j += 32) idx[(int64_t)z * gridDim.x * k + j] = -1;
+                    for (int j = lane; j < k; j += 32) {
+                        idx[(int64_t)z * gridDim.x * k + j] = -1;
+                        if (p) w_out[((int64_t)row + (int64_t)z * gridDim.x) * k + j] = CUDART_NAN_F;
+                    }
                 return;
             }
             const uint16_t *from = All.stage[i & 1];

@@ -54,10 +54,37 @@ assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 @pytest.mark.parametrize("rows,n,k", [(9000, 1501, 9), (100, 3000, 30), (3000, 7000, 40), (1500, 12_003, 100), (700, 30_001, 200),
-                                      (400, 20_000, 1500)])
+                                      (700, 32_768, 1100), (400, 20_000, 1500)])
 @pytest.mark.parametrize("row", [0, 1])
 def test_the_selection_goes_on_from_memory(rows, n, k, row):
     child(SELECTION, rows, n, k, row)
+
+
+WRITING = """
+rows, n, k, row = {}, {}, {}, {}
+r = torch.randn(rows, n, device="cuda")
+p = torch.rand(rows, n, device="cuda")
+idx, w = torch.empty(rows, k, dtype=torch.int32, device="cuda"), torch.empty(rows, k, device="cuda")
+
+def call():
+    idx.fill_(7)
+    w.fill_(0.5)
+    R.select(r, k, p, idx_out=idx, w_out=w)
+    return idx.clone(), w.clone()
+
+want, got = given_up(WRITE, row, call)
+marked = (got[0] == -1).any(dim=1)
+blocks = torch.cuda.get_device_properties(0).multi_processor_count
+turn = torch.arange(rows, device="cuda") // blocks
+assert torch.equal(marked, (turn == row) | (turn == row + 1))      # the rows that had been handed over
+assert (got[0][marked] == -1).all() and torch.isnan(got[1][marked]).all()
+assert torch.equal(got[0][~marked], want[0][~marked]) and torch.equal(got[1][~marked], want[1][~marked])
+"""
+
+
+@pytest.mark.parametrize("rows,n,k,row", [(700, 30_001, 200, 1), (700, 20_000, 1, 0), (150, 32_768, 256, 0)])
+def test_rows_that_nobody_writes_are_marked(rows, n, k, row):
+    child(WRITING, rows, n, k, row)
 
 
 GRADIENT = """
