@@ -305,8 +305,8 @@ def selftest_math(which: int, x: torch.Tensor) -> tuple[torch.Tensor, torch.Tens
 
 
 def selftest_give_up(wait: int, row: int | None):
-    """Checked build: the waits of a kind (0 reads, 1 the writing warp's) report that they gave
-    up from a block's row-th row on; None: as they are."""
+    """Checked build: the waits of a kind (0 reads, 1 the writing warp's, 2 a held row's second
+    one) report that they gave up from a block's row-th row on; None: as they are."""
     _check(lib.lapsum_selftest_give_up(int(wait), 2 ** 31 - 1 if row is None else int(row)), "lapsum_selftest_give_up")
 
 

@@ -8,10 +8,10 @@
 
 namespace lapsum {
 
-enum GiveUp { GIVE_UP_READ = 0, GIVE_UP_WRITE = 1, GIVE_UP_KINDS = 2 };   // LAPSUM_GIVE_UP_*
+enum GiveUp { GIVE_UP_READ = 0, GIVE_UP_WRITE = 1, GIVE_UP_AGAIN = 2, GIVE_UP_KINDS = 3 };   // LAPSUM_GIVE_UP_*
 
 #ifdef LAPSUM_CHECKED
-static __device__ int g_give_up_from[GIVE_UP_KINDS] = {INT_MAX, INT_MAX};   // a block's row from which on its waits give up
+static __device__ int g_give_up_from[GIVE_UP_KINDS] = {INT_MAX, INT_MAX, INT_MAX};   // a block's row from which on its waits give up
 __device__ __forceinline__ bool waited(bool ok, GiveUp kind, int turn) { return ok && turn < g_give_up_from[kind]; }
 static inline cudaError_t set_give_up(GiveUp kind, int turn) {
     return cudaMemcpyToSymbol(g_give_up_from, &turn, sizeof(int), sizeof(int) * kind);

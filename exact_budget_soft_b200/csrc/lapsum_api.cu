@@ -828,7 +828,7 @@ int lapsum_selftest_math(int which, const double *in, double *out, double *ref, 
 
 int lapsum_selftest_give_up(int32_t wait, int32_t row) {
 #ifdef LAPSUM_CHECKED
-    if ((wait != LAPSUM_GIVE_UP_READ && wait != LAPSUM_GIVE_UP_WRITE) || row < 0) return LAPSUM_ERR_ARG;
+    if (wait < LAPSUM_GIVE_UP_READ || wait > LAPSUM_GIVE_UP_AGAIN || row < 0) return LAPSUM_ERR_ARG;
     LAPSUM_TRY(select_give_up(wait, row));
     LAPSUM_TRY(tokens_give_up(wait, row));
     return LAPSUM_OK;

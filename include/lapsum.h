@@ -288,6 +288,7 @@ LAPSUM_API int lapsum_selftest_math(int which, const double *in_dev, double *out
  */
 #define LAPSUM_GIVE_UP_READ  0   /* the wait for a row that is copied into shared memory */
 #define LAPSUM_GIVE_UP_WRITE 1   /* the wait of the warp that writes a long row's selection */
+#define LAPSUM_GIVE_UP_AGAIN 2   /* the second wait for a row that is held, after one that gave up */
 LAPSUM_API int lapsum_selftest_give_up(int32_t wait, int32_t row);
 
 /*

@@ -150,5 +150,5 @@ def test_exports_cover_the_routing_calls():
 def test_waits_give_up_on_request_in_the_checked_build_alone():
     if not L.CHECKED:
         assert L.lib.lapsum_selftest_give_up(0, 1) == L.ERR_ARG
-    for wait, row in ((2, 0), (-1, 0), (0, -1)):
+    for wait, row in ((3, 0), (-1, 0), (0, -1)):
         assert L.lib.lapsum_selftest_give_up(wait, row) == L.ERR_ARG
