@@ -2281,12 +2281,15 @@ using namespace lapsum;
 
 extern "C" {
 
-int64_t lapsum_select_scratch(int64_t rows, int64_t n, int64_t k) {
+// (what a device's launch set-up keeps is host memory: no exception leaves a C entry)
+int64_t lapsum_select_scratch(int64_t rows, int64_t n, int64_t k) try {
     return sel_sizes_ok(rows, n, k) ? (int64_t)sel_scratch(rows, n) : LAPSUM_ERR_ARG;
+} catch (...) {
+    return LAPSUM_ERR_ALLOC;
 }
 
 int lapsum_select(const float *scores, const float *p, int64_t rows, int64_t n, int64_t k, int32_t *idx, float *w,
-                  void *scratch, int64_t scratch_bytes, struct CUstream_st *stream_in) {
+                  void *scratch, int64_t scratch_bytes, struct CUstream_st *stream_in) try {
     if (!scores || !idx || !sel_sizes_ok(rows, n, k) || (p == nullptr) != (w == nullptr)) return LAPSUM_ERR_ARG;
     if (!scratch_ok(scratch, scratch_bytes, sel_scratch(rows, n))) return LAPSUM_ERR_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_in);
@@ -2334,6 +2337,8 @@ int lapsum_select(const float *scores, const float *p, int64_t rows, int64_t n, 
         { Launch L("select_emit", st); LAPSUM_TRY(launch_k(select_emit_kernel, grid, SEL_T, 0, st, A)); }
     }
     return LAPSUM_OK;
+} catch (...) {
+    return LAPSUM_ERR_ALLOC;
 }
 
 int64_t lapsum_select_backward_scratch(int64_t rows, int64_t n) {
@@ -2342,7 +2347,7 @@ int64_t lapsum_select_backward_scratch(int64_t rows, int64_t n) {
 
 int lapsum_select_backward(const float *scores, const double *b, const int32_t *idx, const float *dw, int64_t rows,
                            int64_t n, int64_t k, double t, float *grad, void *scratch, int64_t scratch_bytes,
-                           struct CUstream_st *stream_in) {
+                           struct CUstream_st *stream_in) try {
     if (!scores || !b || !idx || !dw || !grad || !sel_sizes_ok(rows, n, k)) return LAPSUM_ERR_ARG;
     if (!(t >= LAPSUM_T_MIN && t <= LAPSUM_T_MAX)) return LAPSUM_ERR_ARG;
     if (!scratch_ok(scratch, scratch_bytes, grad_scratch(rows, n))) return LAPSUM_ERR_ARG;
@@ -2379,6 +2384,8 @@ int lapsum_select_backward(const float *scores, const double *b, const int32_t *
         { Launch L("select_grad_apply", st); LAPSUM_TRY(launch_k(select_grad_apply_kernel, grid, GL_T, 0, st, A)); }
     }
     return LAPSUM_OK;
+} catch (...) {
+    return LAPSUM_ERR_ALLOC;
 }
 
 }  // extern "C"

@@ -713,8 +713,9 @@ using namespace lapsum;
 
 extern "C" {
 
+// (what a device's launch set-up keeps is host memory: no exception leaves a C entry)
 int lapsum_dispatch(const void *x, int32_t type, int64_t d, const lapsum_route *R, void *out,
-                    struct CUstream_st *stream_in) {
+                    struct CUstream_st *stream_in) try {
     if (!x || !out || !rows_ok(type, d, R) || !aligned(type, {x, out})) return LAPSUM_ERR_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_in);
     const int64_t rb = d * type_size(type);
@@ -724,10 +725,12 @@ int lapsum_dispatch(const void *x, int32_t type, int64_t d, const lapsum_route *
     if (type == LAPSUM_TYPE_F32) LAPSUM_TRY(run_dispatch<uint32_t>(A, vb, st));
     else LAPSUM_TRY(run_dispatch<uint16_t>(A, vb, st));
     return LAPSUM_OK;
+} catch (...) {
+    return LAPSUM_ERR_ALLOC;
 }
 
 int lapsum_dispatch_backward(const void *g, int32_t type, int64_t d, const lapsum_route *R, void *grad_x,
-                             struct CUstream_st *stream_in) {
+                             struct CUstream_st *stream_in) try {
     if (!g || !grad_x || !rows_ok(type, d, R) || !aligned(type, {g, grad_x})) return LAPSUM_ERR_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_in);
     const int64_t rb = d * type_size(type);
@@ -735,10 +738,12 @@ int lapsum_dispatch_backward(const void *g, int32_t type, int64_t d, const lapsu
     Launch L("dispatch_grad", st);
     LAPSUM_TRY(run_to_tokens_type<false>(A, type, vec_bytes(rb, {g, grad_x}), st));
     return LAPSUM_OK;
+} catch (...) {
+    return LAPSUM_ERR_ALLOC;
 }
 
 int lapsum_combine(const void *h, const float *w, int32_t type, int64_t d, const lapsum_route *R, void *y,
-                   struct CUstream_st *stream_in) {
+                   struct CUstream_st *stream_in) try {
     if (!h || !w || !y || !rows_ok(type, d, R) || !aligned(type, {h, y})) return LAPSUM_ERR_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_in);
     const int64_t rb = d * type_size(type);
@@ -747,10 +752,12 @@ int lapsum_combine(const void *h, const float *w, int32_t type, int64_t d, const
     Launch L("combine", st);
     LAPSUM_TRY(run_to_tokens_type<true>(A, type, vec_bytes(rb, {h, y}), st));
     return LAPSUM_OK;
+} catch (...) {
+    return LAPSUM_ERR_ALLOC;
 }
 
 int lapsum_combine_backward(const void *h, const float *w, const void *g, int32_t type, int64_t d,
-                            const lapsum_route *R, void *grad_h, float *grad_w, struct CUstream_st *stream_in) {
+                            const lapsum_route *R, void *grad_h, float *grad_w, struct CUstream_st *stream_in) try {
     if (!h || !w || !g || !grad_h || !grad_w || !rows_ok(type, d, R) || !aligned(type, {h, g, grad_h}))
         return LAPSUM_ERR_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_in);
@@ -768,6 +775,8 @@ int lapsum_combine_backward(const void *h, const float *w, const void *g, int32_
     else if (type == LAPSUM_TYPE_F16) LAPSUM_TRY(run_combine_grad<__half>(A, vb, st));
     else LAPSUM_TRY(run_combine_grad<__nv_bfloat16>(A, vb, st));
     return LAPSUM_OK;
+} catch (...) {
+    return LAPSUM_ERR_ALLOC;
 }
 
 }  // extern "C"

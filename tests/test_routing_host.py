@@ -1,6 +1,9 @@
 """Refusals of the routing and clipping entry points, found on the host before
 anything is enqueued: no GPU is needed, and no pointer is dereferenced."""
 import ctypes as C
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -152,3 +155,56 @@ def test_waits_give_up_on_request_in_the_checked_build_alone():
         assert L.lib.lapsum_selftest_give_up(0, 1) == L.ERR_ARG
     for wait, row in ((3, 0), (-1, 0), (0, -1)):
         assert L.lib.lapsum_selftest_give_up(wait, row) == L.ERR_ARG
+
+
+NO_MEMORY = r"""
+#include <cstdlib>
+#include <new>
+static thread_local bool none = false;
+extern "C" void no_more_memory(int on) { none = on; }
+void *operator new(std::size_t n) {
+    void *p = none ? nullptr : std::malloc(n ? n : 1);
+    if (!p) throw std::bad_alloc();
+    return p;
+}
+void operator delete(void *p) noexcept { std::free(p); }
+void operator delete(void *p, std::size_t) noexcept { std::free(p); }
+"""
+
+NO_MEMORY_CALLS = r"""
+import ctypes as C, sys
+lib, shim = C.CDLL(sys.argv[1]), C.CDLL(None)
+i64, vp = C.c_int64, C.c_void_p
+for name in ("lapsum_select_scratch", "lapsum_route_scratch"):
+    getattr(lib, name).restype = i64
+class Route(C.Structure):
+    _fields_ = [(n, i64) for n in ("tokens", "experts", "slots")] + [(str(i), vp) for i in range(6)]
+F = 0x1000                                     # never dereferenced: nothing can be launched
+p, big = vp(F), i64(1 << 40)
+r = C.byref(Route(4, 3, 8, F, F, F, F, F, F))
+large = C.byref(Route(4000, 3, 8000, F, F, F, F, F, F))
+n = lambda *v: [i64(x) for x in v]
+calls = {
+    "scratch": lambda: lib.lapsum_select_scratch(*n(2, 40000, 5)),
+    "select": lambda: lib.lapsum_select(p, None, *n(2, 2000, 5), p, None, p, big, None),
+    "long": lambda: lib.lapsum_select(p, None, *n(2, 40000, 5), p, None, p, big, None),
+    "backward": lambda: lib.lapsum_select_backward(p, p, p, p, *n(2, 2000, 5), C.c_double(0.1), p, p, big, None),
+    "route": lambda: lib.lapsum_route_build(p, C.c_int32(0), i64(2), r, p, big, None),
+    "combine": lambda: lib.lapsum_combine(p, p, C.c_int32(0), i64(8), r, p, None),
+    "rows": lambda: lib.lapsum_dispatch_backward(p, C.c_int32(0), i64(2048), large, p, None),
+}
+shim.no_more_memory(1)
+code = calls[sys.argv[2]]()
+shim.no_more_memory(0)
+print("code", code)
+"""
+
+
+@pytest.mark.parametrize("call", ["scratch", "select", "long", "backward", "route", "combine", "rows"])
+def test_no_exception_leaves_an_entry_when_host_memory_runs_out(tmp_path, call):
+    (tmp_path / "shim.cpp").write_text(NO_MEMORY)
+    shim = str(tmp_path / "shim.so")
+    subprocess.check_call(["g++", "-O1", "-shared", "-fPIC", "-o", shim, str(tmp_path / "shim.cpp")])
+    out = subprocess.run([sys.executable, "-c", NO_MEMORY_CALLS, L.LIB_PATH, call], capture_output=True, text=True, timeout=120,
+                         env=dict(os.environ, LD_PRELOAD=shim, CUDA_VISIBLE_DEVICES=""))
+    assert out.returncode == 0 and f"code {L.ERR_ALLOC}\n" in out.stdout, (out.returncode, out.stdout, out.stderr[-500:])
