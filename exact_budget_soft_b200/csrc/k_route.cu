@@ -400,6 +400,9 @@ int lapsum_route_build(const int32_t *ids, int32_t by, int64_t k, const lapsum_r
     if (!R->slot_token || !R->slot_entry || !R->expert_offsets || !R->token_offsets || !R->token_slots ||
         !R->token_entries)
         return LAPSUM_ERR_ARG;
+    if (!multiples_of(4, ids, R->slot_token, R->slot_entry, R->expert_offsets, R->token_offsets, R->token_slots,
+                      R->token_entries))
+        return LAPSUM_ERR_ARG;
     if (p.scratch && (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 15) || scratch_bytes < (int64_t)p.scratch))
         return LAPSUM_ERR_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_in);

@@ -2291,6 +2291,7 @@ int64_t lapsum_select_scratch(int64_t rows, int64_t n, int64_t k) try {
 int lapsum_select(const float *scores, const float *p, int64_t rows, int64_t n, int64_t k, int32_t *idx, float *w,
                   void *scratch, int64_t scratch_bytes, struct CUstream_st *stream_in) try {
     if (!scores || !idx || !sel_sizes_ok(rows, n, k) || (p == nullptr) != (w == nullptr)) return LAPSUM_ERR_ARG;
+    if (!multiples_of(4, scores, p, idx, w)) return LAPSUM_ERR_ARG;
     if (!scratch_ok(scratch, scratch_bytes, sel_scratch(rows, n))) return LAPSUM_ERR_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_in);
     if (n <= SEL_CTA_MAX) {
@@ -2349,6 +2350,7 @@ int lapsum_select_backward(const float *scores, const double *b, const int32_t *
                            int64_t n, int64_t k, double t, float *grad, void *scratch, int64_t scratch_bytes,
                            struct CUstream_st *stream_in) try {
     if (!scores || !b || !idx || !dw || !grad || !sel_sizes_ok(rows, n, k)) return LAPSUM_ERR_ARG;
+    if (!multiples_of(4, scores, idx, dw, grad) || !multiples_of(8, b)) return LAPSUM_ERR_ARG;
     if (!(t >= LAPSUM_T_MIN && t <= LAPSUM_T_MAX)) return LAPSUM_ERR_ARG;
     if (!scratch_ok(scratch, scratch_bytes, grad_scratch(rows, n))) return LAPSUM_ERR_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_in);

@@ -556,7 +556,8 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(Rows R) {
 bool route_ok(const lapsum_route *R) {
     const int64_t lim = int64_t(1) << 31;
     return R && R->tokens >= 1 && R->tokens < lim && R->slots >= 1 && R->slots < lim && R->slot_token &&
-           R->token_offsets && R->token_slots && R->token_entries;
+           R->token_offsets && R->token_slots && R->token_entries &&
+           multiples_of(4, R->slot_token, R->token_offsets, R->token_slots, R->token_entries);
 }
 int type_size(int32_t type) {
     return type == LAPSUM_TYPE_F32 ? 4 : type == LAPSUM_TYPE_F16 || type == LAPSUM_TYPE_BF16 ? 2 : 0;
@@ -744,7 +745,7 @@ int lapsum_dispatch_backward(const void *g, int32_t type, int64_t d, const lapsu
 
 int lapsum_combine(const void *h, const float *w, int32_t type, int64_t d, const lapsum_route *R, void *y,
                    struct CUstream_st *stream_in) try {
-    if (!h || !w || !y || !rows_ok(type, d, R) || !aligned(type, {h, y})) return LAPSUM_ERR_ARG;
+    if (!h || !w || !y || !rows_ok(type, d, R) || !aligned(type, {h, y}) || !multiples_of(4, w)) return LAPSUM_ERR_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_in);
     const int64_t rb = d * type_size(type);
     Rows A = make_rows(R, rb, h, R->slots, y);
@@ -758,7 +759,8 @@ int lapsum_combine(const void *h, const float *w, int32_t type, int64_t d, const
 
 int lapsum_combine_backward(const void *h, const float *w, const void *g, int32_t type, int64_t d,
                             const lapsum_route *R, void *grad_h, float *grad_w, struct CUstream_st *stream_in) try {
-    if (!h || !w || !g || !grad_h || !grad_w || !rows_ok(type, d, R) || !aligned(type, {h, g, grad_h}))
+    if (!h || !w || !g || !grad_h || !grad_w || !rows_ok(type, d, R) || !aligned(type, {h, g, grad_h}) ||
+        !multiples_of(4, w, grad_w))
         return LAPSUM_ERR_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_in);
     const int64_t rb = d * type_size(type);

@@ -1,6 +1,7 @@
 // lapsum_launch.h -- what every entry point shares on the host: the launch
 // record, and the mapping of CUDA errors to return codes (internal).
 #pragma once
+#include <cstdint>
 #include <cuda_runtime.h>
 
 #include "../../include/lapsum.h"
@@ -24,6 +25,12 @@ inline int map_err(cudaError_t e) {
     if (e == cudaSuccess) return LAPSUM_OK;
     if (e == cudaErrorMemoryAllocation) return LAPSUM_ERR_ALLOC;
     return LAPSUM_ERR_CUDA;
+}
+
+// Addresses that are multiples of `to`, a power of two (null is one).
+template <typename... P>
+inline bool multiples_of(uintptr_t to, P... p) {
+    return ((reinterpret_cast<uintptr_t>(p) | ...) & (to - 1)) == 0;
 }
 
 #define LAPSUM_TRY(expr)                                    \

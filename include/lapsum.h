@@ -423,7 +423,8 @@ LAPSUM_API int lapsum_shard_vjp_apply(const float *scores_dev, const double *b_d
  * *_scratch function returns, 16-byte aligned, private to the call until it has
  * run).  They may be captured into graphs, and calls on different streams are
  * independent when their scratch and outputs are.  Results do not depend on the
- * order in which blocks run.
+ * order in which blocks run.  An address that is not a multiple of its type's
+ * size is refused (LAPSUM_ERR_ARG).
  */
 #define LAPSUM_TYPE_F32  0
 #define LAPSUM_TYPE_F16  1

@@ -208,3 +208,29 @@ def test_no_exception_leaves_an_entry_when_host_memory_runs_out(tmp_path, call):
     out = subprocess.run([sys.executable, "-c", NO_MEMORY_CALLS, L.LIB_PATH, call], capture_output=True, text=True, timeout=120,
                          env=dict(os.environ, LD_PRELOAD=shim, CUDA_VISIBLE_DEVICES=""))
     assert out.returncode == 0 and f"code {L.ERR_ALLOC}\n" in out.stdout, (out.returncode, out.stdout, out.stderr[-500:])
+
+
+def off(at, count, by=2):
+    return [F + by if i == at else F for i in range(count)]
+
+
+def test_addresses_off_their_types_are_refused():
+    for at in range(4):
+        scores, p, idx, w = off(at, 4)
+        assert L.lib.lapsum_select(scores, p, 1, 8, 2, idx, w, F, BIG, None) == L.ERR_ARG
+    for at, by in ((0, 2), (1, 2), (1, 4), (2, 2), (3, 2), (4, 2)):
+        scores, b, idx, dw, grad = off(at, 5, by)
+        assert L.lib.lapsum_select_backward(scores, b, idx, dw, 1, 8, 2, 0.1, grad, F, BIG, None) == L.ERR_ARG
+    assert L.lib.lapsum_route_build(F + 2, 0, 2, route(), F, BIG, None) == L.ERR_ARG
+    arrays = ("slot_token", "slot_entry", "expert_offsets", "token_offsets", "token_slots", "token_entries")
+    for name in arrays:
+        assert L.lib.lapsum_route_build(F, 0, 2, route(**{name: F + 2}), F, BIG, None) == L.ERR_ARG
+    for name in (arrays[0], *arrays[3:]):          # the arrays that the row passes read
+        r = route(**{name: F + 2})
+        assert L.lib.lapsum_dispatch(F, 0, 8, r, F, None) == L.ERR_ARG
+        assert L.lib.lapsum_dispatch_backward(F, 0, 8, r, F, None) == L.ERR_ARG
+        assert L.lib.lapsum_combine(F, F, 0, 8, r, F, None) == L.ERR_ARG
+        assert L.lib.lapsum_combine_backward(F, F, F, 0, 8, r, F, F, None) == L.ERR_ARG
+    assert L.lib.lapsum_combine(F, F + 2, 0, 8, route(), F, None) == L.ERR_ARG
+    assert L.lib.lapsum_combine_backward(F, F + 2, F, 0, 8, route(), F, F, None) == L.ERR_ARG
+    assert L.lib.lapsum_combine_backward(F, F, F, 0, 8, route(), F, F + 2, None) == L.ERR_ARG
