@@ -30,14 +30,19 @@ def clip_grads(grads, max_norm: float, outs=None, norm_out: torch.Tensor | None 
     """norm = sqrt(sum of all squares) of the tensors in `grads` (float32, float16 or
     bfloat16, contiguous, on one GPU), as a float32 scalar tensor; each is multiplied by
     min(1, max_norm / (norm + 1e-6)) into `outs` (default: in place).  max_norm may be
-    infinite: the norm alone.  The squares of a 16-byte vector are summed in 32 bits, the
+    infinite: the norm alone.  A None among grads, of a parameter that took no part, is
+    skipped (with its place in outs).  The squares of a 16-byte vector are summed in 32 bits, the
     rest in 64, in an order fixed by the sizes and alignments."""
-    grads = list(grads)
+    given = list(grads)
+    grads = [g for g in given if g is not None]
     if not grads:
         raise ValueError("grads must hold at least one tensor")
     outs = grads if outs is None else list(outs)
-    if len(outs) != len(grads):
-        raise ValueError(f"outs must hold {len(grads)} tensors, not {len(outs)}")
+    if outs is not grads:
+        if len(outs) != len(given):
+            raise ValueError(f"outs must hold {len(given)} tensors, not {len(outs)}")
+        if len(grads) != len(given):
+            outs = [o for g, o in zip(given, outs) if g is not None]
     if not max_norm >= 0:
         raise ValueError(f"max_norm must be 0 or more, not {max_norm}")
     dev = grads[0].device

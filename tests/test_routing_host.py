@@ -234,3 +234,13 @@ def test_addresses_off_their_types_are_refused():
     assert L.lib.lapsum_combine(F, F + 2, 0, 8, route(), F, None) == L.ERR_ARG
     assert L.lib.lapsum_combine_backward(F, F + 2, F, 0, 8, route(), F, F, None) == L.ERR_ARG
     assert L.lib.lapsum_combine_backward(F, F, F, 0, 8, route(), F, F + 2, None) == L.ERR_ARG
+
+
+def test_clip_refuses_a_list_without_a_gradient():
+    for none in ([None], [None, None]):
+        with pytest.raises(ValueError, match="at least one"):
+            grads.clip_grads(none, 1.0)
+    with pytest.raises(ValueError, match="outs"):
+        grads.clip_grads([None, torch.zeros(3)], 1.0, outs=[torch.zeros(3)])
+    with pytest.raises(ValueError, match="CUDA"):
+        grads.clip_grads([None, torch.zeros(3)], 1.0)
