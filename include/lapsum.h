@@ -511,10 +511,12 @@ LAPSUM_API int lapsum_combine_backward(const void *h_dev, const float *w_dev, co
 
 /*
  * Clipping by the global norm.  norm = sqrt(sum of all squares over `count`
- * tensors), out = grad * min(1, max_norm / (norm + 1e-6)), rounded once.  The
- * squares of a 16-byte vector are summed in fp32 (in fp64 where they would
- * overflow or vanish), the rest in fp64.  The VJP of this library grows as 1/t: a step that anneals
- * t clips.
+ * tensors), out = grad * min(1, max_norm / (norm + 1e-6)).  The squares of a
+ * 16-byte vector are summed in fp32 (in fp64 where they would overflow or
+ * vanish), the rest in fp64.  The factor is formed in fp64 and rounded to fp32,
+ * its product with a value to fp32, and that to the output's type (16 bits: a
+ * third rounding).  The VJP of this library grows as 1/t: a step that anneals t
+ * clips.
  *   grads   host array of device pointers; sizes: values of each (0 is allowed);
  *   types   LAPSUM_TYPE_* of each (grad and out alike)
  *   outs    host array of device pointers: each outs[i] equals grads[i] (in place)
