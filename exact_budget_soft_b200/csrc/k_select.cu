@@ -430,19 +430,17 @@ __device__ __forceinline__ void rs_marked(RowState<G, B> &S, const Member<G> &M,
         for (uint32_t m = g[q] | e[q]; m; m &= m - 1) put(o++, (first + q) * 32 + __ffs(m) - 1);
 }
 
-// Writes the row's selection.  A short one passes through the lists' room, so that
-// its gate values are fetched together.
+// Writes the row's selection through the lists' room, so that its gate values are fetched
+// together.  (k is no more than the room: row_rank sends larger ones to the held rows.)
 template <int G>
 __device__ __forceinline__ void rs_emit(RowGroup<G> &S, const Member<G> &M, unsigned need, int k, const float *p, int32_t *idx,
                                         float *w) {
-    const bool staged = k <= G * RS_LIST;
-    int32_t *to = staged ? reinterpret_cast<int32_t *>(&S.key[0][0]) : idx;
+    int32_t *to = reinterpret_cast<int32_t *>(&S.key[0][0]);
     rs_marked(S, M, need, [&](unsigned o, int i) { to[o] = i; });
-    if (!staged && !p) return;
     M.sync();
     for (int j = M.tid; j < k; j += 32 * G) {
-        const int i = staged ? to[j] : __ldcg(idx + j);
-        if (staged) idx[j] = i;
+        const int i = to[j];
+        idx[j] = i;
         if (p) w[j] = p[i];
     }
 }
@@ -1799,19 +1797,14 @@ __device__ __forceinline__ bool idx_ok(const int32_t *idx, int64_t j, int64_t n)
     return i >= 0 && i < n && (j == 0 || idx[j - 1] < i);
 }
 
-// T threads a row (a warp, or a CTA of T): the row's |x| in I registers a thread.
-// Rows of up to 1024 scores.
-template <int T, int I>
-__global__ void __launch_bounds__(T == 32 ? 256 : T)
+// A warp a row, its |x| in I registers a lane.  Rows of up to 1024 scores.
+template <int I>
+__global__ void __launch_bounds__(256)
 select_grad_kernel(const float *__restrict__ scores, const double *__restrict__ b_in, const int32_t *__restrict__ idx_in,
                    const float *__restrict__ dw_in, int64_t rows, int n, int k, double inv_t, float *__restrict__ grad) {
-    constexpr int NW = T / 32;
-    __shared__ GradAcc s_acc[NW];
-    __shared__ float s_m[NW];
     pdl_enter();
-    const int tid = T == 32 ? (threadIdx.x & 31) : threadIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = T == 32 ? (int64_t)blockIdx.x * 8 + warp : blockIdx.x;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (row >= rows) return;
     const float *r = scores + row * n;
     const int32_t *idx = idx_in + row * k;
@@ -1822,49 +1815,32 @@ select_grad_kernel(const float *__restrict__ scores, const double *__restrict__ 
     float m = CUDART_INF_F;
 #pragma unroll
     for (int j = 0; j < I; ++j) {
-        const int i = j * T + tid;
+        const int i = j * 32 + lane;
         ax[j] = i < n ? ax_of(xf, r[i]) : CUDART_INF_F;
         m = min_nan(m, ax[j]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = min_nan(m, __shfl_xor_sync(FULL, m, o));
-    if (T > 32) {
-        if (lane == 0) s_m[warp] = m;
-        __syncthreads();
-        for (int w = 0; w < NW; ++w) m = min_nan(m, s_m[w]);
-    }
-    GradAcc a{m, 0.0, 0.0};
+    double sg = 0.0;
     float sf = 0.f;
 #pragma unroll
     for (int j = 0; j < I; ++j) sf += exp2f(m - ax[j]);   // places behind the row: 2^-inf = 0
-    a.sf = (double)sf;
     bool bad = false;
-    for (int j = tid; j < k; j += T) {
-        if (idx_ok(idx, j, n)) a.sg += (double)dw[j] * (double)exp2f(m - ax_of(xf, r[idx[j]]));
+    for (int j = lane; j < k; j += 32) {
+        if (idx_ok(idx, j, n)) sg += (double)dw[j] * (double)exp2f(m - ax_of(xf, r[idx[j]]));
         else bad = true;
     }
-    if (bad) a.sg = CUDART_NAN;
-    a.sf = warp_sum(a.sf);
-    a.sg = warp_sum(a.sg);
-    if (T > 32) {
-        if (lane == 0) s_acc[warp] = a;
-        __syncthreads();
-        a = s_acc[0];
-        for (int w = 1; w < NW; ++w) {
-            a.sf += s_acc[w].sf;
-            a.sg += s_acc[w].sg;
-        }
-    }
-    const double lam = a.sg / a.sf;
+    if (bad) sg = CUDART_NAN;
+    const double lam = warp_sum(sg) / warp_sum((double)sf);
     const GradRow G(lam, inv_t);
 #pragma unroll
     for (int j = 0; j < I; ++j) {
-        const int i = j * T + tid;
+        const int i = j * 32 + lane;
         if (i < n) out[i] = G(ax[j], 0.f);
     }
     if (lam != lam) return;   // also: an index may be out of range
-    if (T == 32) __syncwarp(); else __syncthreads();
-    for (int j = tid; j < k; j += T) out[idx[j]] = G(ax_of(xf, r[idx[j]]), dw[j]);
+    __syncwarp();
+    for (int j = lane; j < k; j += 32) out[idx[j]] = G(ax_of(xf, r[idx[j]]), dw[j]);
 }
 
 // Rows of up to 2048 G scores, G warps a row, read once: one more warp keeps a ring of
@@ -2265,11 +2241,11 @@ cudaError_t run_grad_ring(const float *s, const double *b, const int32_t *idx, c
     return launch_k(kern, (unsigned)std::min<int64_t>(rows, ctas), 32 * G + 32, sizeof(GradShared<G>), st, s, b, idx, dw,
                     (int)rows, (int)n, (int)k, inv_t, grad);
 }
-template <int T, int I>
+template <int I>
 cudaError_t run_grad(const float *s, const double *b, const int32_t *idx, const float *dw, int64_t rows, int64_t n,
                      int64_t k, double inv_t, float *grad, cudaStream_t st) {
-    return launch_k(select_grad_kernel<T, I>, (unsigned)(T == 32 ? (rows + 7) / 8 : rows), T == 32 ? 256 : T, 0, st, s, b,
-                    idx, dw, rows, (int)n, (int)k, inv_t, grad);
+    return launch_k(select_grad_kernel<I>, (unsigned)((rows + 7) / 8), 256, 0, st, s, b, idx, dw, rows, (int)n, (int)k, inv_t,
+                    grad);
 }
 
 }  // namespace
@@ -2358,8 +2334,8 @@ int lapsum_select_backward(const float *scores, const double *b, const int32_t *
     if (n <= SEL_CTA_MAX) {
         Launch L("select_grad", st);
         cudaError_t e;
-        if (n <= 128) e = run_grad<32, 4>(scores, b, idx, dw, rows, n, k, inv_t, grad, st);
-        else if (n <= 1024) e = run_grad<32, 32>(scores, b, idx, dw, rows, n, k, inv_t, grad, st);
+        if (n <= 128) e = run_grad<4>(scores, b, idx, dw, rows, n, k, inv_t, grad, st);
+        else if (n <= 1024) e = run_grad<32>(scores, b, idx, dw, rows, n, k, inv_t, grad, st);
         else if (n <= 2048) e = run_grad_ring<1>(scores, b, idx, dw, rows, n, k, inv_t, grad, st);
         else if (n <= 4096) e = run_grad_ring<2>(scores, b, idx, dw, rows, n, k, inv_t, grad, st);
         else if (n <= 8192) e = run_grad_ring<4>(scores, b, idx, dw, rows, n, k, inv_t, grad, st);

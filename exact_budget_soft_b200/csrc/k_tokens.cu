@@ -45,7 +45,7 @@ struct Rows {
     Span sa, sb;                  // of the inputs
     int64_t row_bytes;
     int64_t tokens, slots;
-    const int32_t *slot_token, *slot_entry, *token_offsets, *token_slots, *token_entries;
+    const int32_t *slot_token, *token_offsets, *token_slots, *token_entries;
 };
 
 // Bytes of a vector; SHIFTED: granules of 16, shifted into place.
@@ -612,7 +612,6 @@ Rows make_rows(const lapsum_route *R, int64_t row_bytes, const void *a, int64_t 
     A.tokens = R->tokens;
     A.slots = R->slots;
     A.slot_token = R->slot_token;
-    A.slot_entry = R->slot_entry;
     A.token_offsets = R->token_offsets;
     A.token_slots = R->token_slots;
     A.token_entries = R->token_entries;
