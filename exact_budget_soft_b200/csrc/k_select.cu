@@ -1749,22 +1749,17 @@ bool sel_sizes_ok(int64_t rows, int64_t n, int64_t k) {
 }
 
 // ---------------------------------------------------------- the gradient --
-// The smaller one; a NaN, where one is (fminf drops it).
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float m;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
-    return m;
-}
-// A shifted pair of sums: sum e and sum dw e with e = 2^{m - |x|}.  A NaN score or
-// threshold stays in m, and so makes both sums and the row's whole gradient NaN.
+// |x| may overflow fp32 (t tiny): it is no more than this, which keeps the shift finite.
+constexpr float AX_MAX = 3.0e38f;
+// A shifted pair of sums: sum e and sum dw e with e = 2^{m - |x|}; m is AX_MAX before the
+// first score.  A NaN score or threshold is not in m, but makes its e NaN, and so the sums
+// and the row's whole gradient.
 struct GradAcc {
     float m;
     double sf, sg;
 };
 __device__ __forceinline__ GradAcc ga_merge(GradAcc a, GradAcc b) {
-    if (b.m == CUDART_INF_F) return a;
-    if (a.m == CUDART_INF_F) return b;
-    const float m = min_nan(a.m, b.m);
+    const float m = fminf(a.m, b.m);
     const double fa = (double)exp2f(m - a.m), fb = (double)exp2f(m - b.m);
     return {m, a.sf * fa + b.sf * fb, a.sg * fa + b.sg * fb};
 }
@@ -1778,7 +1773,9 @@ __device__ __forceinline__ GradAcc ga_warp(GradAcc a) {
     return a;
 }
 __device__ __forceinline__ float ax_of(const XForm &xf, float r) {
-    return min_nan(fabsf(xf(r)), 3.0e38f);   // |x| may overflow fp32 (t tiny): keep the shift finite
+    float a;                               // (fminf would drop a NaN)
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(fabsf(xf(r))), "f"(AX_MAX));
+    return a;
 }
 
 struct GradRow {
@@ -1817,10 +1814,10 @@ select_grad_kernel(const float *__restrict__ scores, const double *__restrict__ 
     for (int j = 0; j < I; ++j) {
         const int i = j * 32 + lane;
         ax[j] = i < n ? ax_of(xf, r[i]) : CUDART_INF_F;
-        m = min_nan(m, ax[j]);
+        m = fminf(m, ax[j]);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = min_nan(m, __shfl_xor_sync(FULL, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = fminf(m, __shfl_xor_sync(FULL, m, o));
     double sg = 0.0;
     float sf = 0.f;
 #pragma unroll
@@ -1914,15 +1911,17 @@ select_grad_ring_kernel(const float *__restrict__ scores, const double *__restri
         // the scores outside the granules: at most one a lane of the first warp
         const int edge = warp ? -1 : lane < 4 ? (lane < head ? lane : -1) : (head + body + lane - 4 < n ? head + body + lane - 4 : -1);
         const float edge_ax = edge >= 0 ? ax_of(xf, r[edge]) : CUDART_INF_F;
-        float m = edge_ax;
-        double sf = edge >= 0 ? 1.0 : 0.0;
+        const float edge_m = fminf(edge_ax, AX_MAX);
+        const double edge_sf = edge >= 0 ? (double)exp2f(edge_m - edge_ax) : 0.0;
+        float m = edge_m;
+        double sf = edge_sf;
         auto add = [&](const float (&ax)[8]) {
             float lm = ax[0];
 #pragma unroll
-            for (int i = 1; i < 8; ++i) lm = min_nan(lm, ax[i]);
-            if (!(lm >= m)) {              // (once NaN: m stays it)
-                sf *= m == CUDART_INF_F ? 0.0 : (double)exp2f(lm - m);
-                m = min_nan(m, lm);
+            for (int i = 1; i < 8; ++i) lm = fminf(lm, ax[i]);
+            if (lm < m) {
+                sf *= (double)exp2f(lm - m);
+                m = lm;
             }
             float s = 0.f;
 #pragma unroll
@@ -1960,7 +1959,7 @@ select_grad_ring_kernel(const float *__restrict__ scores, const double *__restri
         // the smallest |x| of the row
         float wm = m;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) wm = min_nan(wm, __shfl_xor_sync(FULL, wm, o));
+        for (int o = 16; o > 0; o >>= 1) wm = fminf(wm, __shfl_xor_sync(FULL, wm, o));
         const bool warp_bad = __any_sync(FULL, !ok);
         if (lane == 0) {
             S.m[warp] = wm;
@@ -1971,13 +1970,13 @@ select_grad_ring_kernel(const float *__restrict__ scores, const double *__restri
         int gave_up = S.bad[0];
 #pragma unroll
         for (int w = 1; w < G; ++w) {
-            lo = min_nan(lo, S.m[w]);
+            lo = fminf(lo, S.m[w]);
             gave_up |= S.bad[w];
         }
         if (gave_up || !ring) {            // this row and the later ones from memory
             ring = false;
-            m = edge_ax;
-            sf = edge >= 0 ? 1.0 : 0.0;
+            m = edge_m;
+            sf = edge_sf;
             for (int a = 0; a < body; a += CHUNK) {
                 float ax[8];
                 eight(0, a, ax);
@@ -1985,13 +1984,13 @@ select_grad_ring_kernel(const float *__restrict__ scores, const double *__restri
             }
             lo = m;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) lo = min_nan(lo, __shfl_xor_sync(FULL, lo, o));
+            for (int o = 16; o > 0; o >>= 1) lo = fminf(lo, __shfl_xor_sync(FULL, lo, o));
             M.sync();
             if (lane == 0) S.m[warp] = lo;
             M.sync();
-            for (int w = 0; w < G; ++w) lo = min_nan(lo, S.m[w]);
+            for (int w = 0; w < G; ++w) lo = fminf(lo, S.m[w]);
         }
-        sf = m == CUDART_INF_F ? 0.0 : sf * (double)exp2f(lo - m);
+        sf *= (double)exp2f(lo - m);
         // the selected scores' part, out of the ring
         auto ax_at = [&](int i) -> float {
             const int o = i - head;
@@ -2129,7 +2128,7 @@ __global__ void __launch_bounds__(GL_T) select_grad_sum_kernel(GradLong L) {
     const float *dw = L.dw + row * L.k;
     const XForm xf = make_xform(L.b[row], L.inv_t * LOG2E);
     const int64_t a0 = (int64_t)blockIdx.x * L.chunk, a1 = min(a0 + L.chunk, L.n);
-    GradAcc acc{CUDART_INF_F, 0.0, 0.0};
+    GradAcc acc{AX_MAX, 0.0, 0.0};
     for (int64_t i0 = a0; i0 < a1; i0 += 8 * GL_T) {
         float ax[8];
         float m = acc.m;
@@ -2137,11 +2136,10 @@ __global__ void __launch_bounds__(GL_T) select_grad_sum_kernel(GradLong L) {
         for (int q = 0; q < 8; ++q) {
             const int64_t i = i0 + q * GL_T + threadIdx.x;
             ax[q] = i < a1 ? ax_of(xf, r[i]) : CUDART_INF_F;
-            m = min_nan(m, ax[q]);
+            m = fminf(m, ax[q]);
         }
-        if (m == CUDART_INF_F) continue;
-        if (!(m >= acc.m)) {
-            if (acc.m != CUDART_INF_F) acc.sf *= (double)exp2f(m - acc.m);
+        if (m < acc.m) {
+            acc.sf *= (double)exp2f(m - acc.m);
             acc.m = m;
         }
         float s = 0.f;
@@ -2157,7 +2155,7 @@ __global__ void __launch_bounds__(GL_T) select_grad_sum_kernel(GradLong L) {
         if (!idx_ok(idx, j, L.n)) { bad = true; continue; }
         const float ax = ax_of(xf, r[idx[j]]);
         if (ax < acc.m) {
-            const double sc = acc.m == CUDART_INF_F ? 0.0 : (double)exp2f(ax - acc.m);
+            const double sc = (double)exp2f(ax - acc.m);
             acc.sf *= sc;
             acc.sg *= sc;
             acc.m = ax;
@@ -2179,7 +2177,7 @@ __global__ void __launch_bounds__(GL_T) select_grad_apply_kernel(GradLong L) {
     const float *dw = L.dw + row * L.k;
     float *out = L.grad + row * L.n;
     const XForm xf = make_xform(L.b[row], L.inv_t * LOG2E);
-    GradAcc acc{CUDART_INF_F, 0.0, 0.0};
+    GradAcc acc{AX_MAX, 0.0, 0.0};
     for (int c = threadIdx.x; c < L.chunks; c += GL_T) acc = ga_merge(acc, L.part[row * L.chunks + c]);
     acc = ga_block(acc, s_acc);
     const double lam = acc.sg / acc.sf;
