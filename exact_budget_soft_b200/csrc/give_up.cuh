@@ -8,6 +8,14 @@
 
 namespace lapsum {
 
+// Polls of a ring's wait before it gives up: seconds (a poll that finds nothing takes about
+// 1.5 us), 0.1 s in the checked build, whose tests let waits run out.
+#ifdef LAPSUM_CHECKED
+constexpr int RING_WAIT_CAP = 1 << 16;
+#else
+constexpr int RING_WAIT_CAP = BULK_WAIT_CAP;
+#endif
+
 enum GiveUp { GIVE_UP_READ = 0, GIVE_UP_WRITE = 1, GIVE_UP_AGAIN = 2, GIVE_UP_KINDS = 3 };   // LAPSUM_GIVE_UP_*
 
 #ifdef LAPSUM_CHECKED

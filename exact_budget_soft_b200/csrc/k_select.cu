@@ -166,7 +166,7 @@ struct RowShared {
 // The wait of a whole warp, the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int times = 1) {
     bool ok = false;
-    for (int z = 0; z < times && !ok; ++z) ok = mbar_wait(bar, parity, BULK_WAIT_CAP);
+    for (int z = 0; z < times && !ok; ++z) ok = mbar_wait(bar, parity, RING_WAIT_CAP);
     return __all_sync(FULL, ok);
 }
 
@@ -465,7 +465,7 @@ __device__ __forceinline__ void rs_stream(float (*ring)[CHUNK], uint64_t *full, 
         int head, body;
         rs_granules(r, n, head, body);
         for (int a = 0; a < body; a += CHUNK) {
-            ok = mbar_wait(&empty[slot], phase, BULK_WAIT_CAP);
+            ok = mbar_wait(&empty[slot], phase, RING_WAIT_CAP);
             if (!ok) break;
             const uint32_t bytes = (uint32_t)min(CHUNK, body - a) * 4u;
             fence_proxy_async_smem();
@@ -480,7 +480,7 @@ __device__ __forceinline__ void rs_stream(float (*ring)[CHUNK], uint64_t *full, 
     // no CTA ends with copies in flight: the last of every slot
     for (uint32_t z = 0; z < min(sent, (uint32_t)RING); ++z) {
         const uint32_t seq = sent - 1 - z;
-        mbar_wait(&full[seq % RING], (seq / RING) & 1, BULK_WAIT_CAP);
+        mbar_wait(&full[seq % RING], (seq / RING) & 1, RING_WAIT_CAP);
     }
 }
 
@@ -933,7 +933,7 @@ select_wide_kernel(const float *__restrict__ scores, const float *__restrict__ p
         if (M.lane == 0) S.scan[M.warp] = got;
         if (M.tid == 0) {
             const bool was = hand;
-            All.handed[buf] = hand = hand && mbar_wait(&All.stage_empty[buf], ((i >> 1) & 1) ^ 1, BULK_WAIT_CAP);
+            All.handed[buf] = hand = hand && mbar_wait(&All.stage_empty[buf], ((i >> 1) & 1) ^ 1, RING_WAIT_CAP);
             if (was && !hand) All.direct[buf] = i;
         }
         M.sync();
@@ -993,7 +993,7 @@ select_wide_kernel(const float *__restrict__ scores, const float *__restrict__ p
 // scores of it two ranks, four standard deviations to either side of k's, bracket A.
 // One pass counts the keys above the bracket and a histogram within it, one marks; more
 // only for ties and about zero, where keys lie far apart.  The next row is fetched while
-// this one is written, 32 places a warp.  (2^25 scores, k = n / 4: 160, 154, 132 and 143 us
+// this one is written, 32 places a warp.  (2^25 scores, k = n / 4: 162, 155, 132 and 143 us
 // at n = 2048, 4096, 16384 and 32768; with four passes over the row in memory, on all key
 // bits, 242, 305, 311 and 283.)  Bound by the passes' instructions: the SM issues in 81 of
 // 100 cycles.
@@ -1073,11 +1073,11 @@ select_held_kernel(const float *__restrict__ scores, const float *__restrict__ p
             H.lo = 0xffffffffu;
             H.hi = 0xff800000u;            // +infinity
         }
-        const bool ok = !bulk || waited(mbar_wait(&H.bar, phase, BULK_WAIT_CAP), GIVE_UP_READ, turn);
+        const bool ok = !bulk || waited(mbar_wait(&H.bar, phase, RING_WAIT_CAP), GIVE_UP_READ, turn);
         if (!__syncthreads_and(ok)) {
             // a copy that is late may still write to the only room there is: then this block's rows
             // from here on are marked, and none of them is left stale
-            if (!__syncthreads_and(waited(mbar_wait(&H.bar, phase, BULK_WAIT_CAP), GIVE_UP_AGAIN, turn))) {
+            if (!__syncthreads_and(waited(mbar_wait(&H.bar, phase, RING_WAIT_CAP), GIVE_UP_AGAIN, turn))) {
                 rh_mark((int)row, rows, k, idx_out, p ? w_out : nullptr);
                 return;
             }
@@ -1844,7 +1844,7 @@ select_grad_kernel(const float *__restrict__ scores, const double *__restrict__ 
 // chunks full, which holds a row and more than half of the next one.  The first pass
 // over the row's chunks adds up, the second one writes and leaves them free, so the
 // next row arrives meanwhile.  (One row a CTA in registers, n = 32768: nothing was
-// read while a row was written; 86 us for 1024 rows, this 73 us.)
+// read while a row was written; 86 us for 1024 rows, this 72 us.)
 constexpr int SG_RING = 13;
 template <int G>
 struct GradShared {
@@ -1947,7 +1947,7 @@ select_grad_ring_kernel(const float *__restrict__ scores, const double *__restri
         bool ok = true;
         if (ring)                          // the whole row first: a wait that gives up is then known to all
             for (int a = 0; a < body; a += CHUNK) {
-                ok = ok && waited(mbar_wait(&S.full[slot], phase, BULK_WAIT_CAP), GIVE_UP_READ, turn);
+                ok = ok && waited(mbar_wait(&S.full[slot], phase, RING_WAIT_CAP), GIVE_UP_READ, turn);
                 if (ok) {
                     float ax[8];
                     eight(slot, a, ax);

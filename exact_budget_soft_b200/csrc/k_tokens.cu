@@ -333,7 +333,7 @@ to_tokens_ring_kernel(const __grid_constant__ Rows R, int seg_bytes, int segs) {
                 const int cnt = (int)min(count - p0, (int64_t)32);
                 for (int q = 0; q < cnt; ++q) {
                     if (lane == q && ok) {
-                        ok = mbar_wait(&S.empty[stage], phase, BULK_WAIT_CAP);
+                        ok = mbar_wait(&S.empty[stage], phase, RING_WAIT_CAP);
                         if (ok) {
                             uint4 x = note;
                             x.w |= (p0 + q == 0 ? NOTE_FIRST : 0u) | (p0 + q + 1 == count ? NOTE_LAST : 0u);
@@ -360,7 +360,7 @@ to_tokens_ring_kernel(const __grid_constant__ Rows R, int seg_bytes, int segs) {
         if (lane == 0)
             for (uint32_t z = 0; z < min(sent, (uint32_t)TS_RING); ++z) {
                 const uint32_t q = sent - 1 - z;
-                mbar_wait(&S.full[q % TS_RING], (q / TS_RING) & 1, BULK_WAIT_CAP);
+                mbar_wait(&S.full[q % TS_RING], (q / TS_RING) & 1, RING_WAIT_CAP);
             }
         return;
     }
@@ -375,7 +375,7 @@ to_tokens_ring_kernel(const __grid_constant__ Rows R, int seg_bytes, int segs) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) acc[i] = 0.f;
         for (bool last = false; !last;) {
-            ok = ok && waited(mbar_wait(&S.full[stage], phase, BULK_WAIT_CAP), GIVE_UP_READ, turn);
+            ok = ok && waited(mbar_wait(&S.full[stage], phase, RING_WAIT_CAP), GIVE_UP_READ, turn);
             if (!ok) break;
             const uint4 note = S.note[stage];
             const float w = __uint_as_float(note.z);

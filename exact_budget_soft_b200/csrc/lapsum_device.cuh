@@ -406,13 +406,7 @@ __device__ __forceinline__ float4 lds128(const float4 *p) {
 }
 
 constexpr int BULK_F4 = 512;                    // float4 per source per chunk (8 KB)
-// polls of a wait before it gives up: seconds (a poll that finds nothing takes about
-// 1.5 us), 0.1 s in the checked build, whose tests let waits run out
-#ifdef LAPSUM_CHECKED
-constexpr int BULK_WAIT_CAP = 1 << 16;
-#else
 constexpr int BULK_WAIT_CAP = 1 << 22;
-#endif
 // stages in flight: 4 chunks of one source, 3 of two (48 KB per CTA, so four
 // CTAs of either kind fit one SM's shared memory)
 template <int NSRC>

@@ -119,8 +119,4 @@ int sort_grid_max();
 int64_t sort_record_doubles(int64_t cap);
 cudaError_t launch_radix_sort(SortArgs &A, double k, double t, cudaStream_t st);
 
-// checked build: waits of a kind (GiveUp) report that they gave up from a block's row `turn` on
-cudaError_t select_give_up(int kind, int turn);   // k_select.cu
-cudaError_t tokens_give_up(int kind, int turn);   // k_tokens.cu
-
 }  // namespace lapsum

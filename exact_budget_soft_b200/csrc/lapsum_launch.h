@@ -33,6 +33,10 @@ inline bool multiples_of(uintptr_t to, P... p) {
     return ((reinterpret_cast<uintptr_t>(p) | ...) & (to - 1)) == 0;
 }
 
+// checked build: waits of a kind (GiveUp) report that they gave up from a block's row `turn` on
+cudaError_t select_give_up(int kind, int turn);   // k_select.cu
+cudaError_t tokens_give_up(int kind, int turn);   // k_tokens.cu
+
 #define LAPSUM_TRY(expr)                                    \
     do {                                                    \
         cudaError_t _e = (expr);                            \
