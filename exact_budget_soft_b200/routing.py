@@ -20,6 +20,9 @@ Results are the same on every run.  No step keeps a workspace in the library, so
 all but ``soft_gate`` (its solver has one per stream) may be captured into graphs
 that run side by side.  A captured backward pass needs, as in all of torch, that no
 eager graph of the same leaves is alive meanwhile; the ``*_backward`` steps do not.
+A step given a ``stream`` runs there and its results belong to it; its inputs have to
+live, and to be ready, for that stream (``record_stream``, ``wait_stream``), as in all of
+torch.  Tables, rows and lists hold at least one of each: an empty batch is refused.
 """
 from __future__ import annotations
 
@@ -159,7 +162,8 @@ class _SoftGate(torch.autograd.Function):
 
 def soft_gate(scores: torch.Tensor, k: int, t: float, opts: L.Options | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """(w, idx), both [rows, k]: the k best scores of every row and their soft prices, the
-    prices differentiable in the scores (the whole row's: the budget ties them together)."""
+    prices differentiable in the scores (the whole row's: the budget ties them together).
+    As for ``forward``, the scores are finite and 0 < k < n."""
     return _SoftGate.apply(scores, k, t, opts)
 
 

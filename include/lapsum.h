@@ -424,7 +424,10 @@ LAPSUM_API int lapsum_shard_vjp_apply(const float *scores_dev, const double *b_d
  * run).  They may be captured into graphs, and calls on different streams are
  * independent when their scratch and outputs are.  Results do not depend on the
  * order in which blocks run.  An address that is not a multiple of its type's
- * size is refused (LAPSUM_ERR_ARG).
+ * size is refused (LAPSUM_ERR_ARG).  Waits inside the kernels are bounded (some
+ * seconds); where one gives up a row is read from memory or marked, never left
+ * as it was: indices of -1 and weights of NaN (lapsum_select), NaN
+ * (lapsum_combine, lapsum_dispatch_backward).
  */
 #define LAPSUM_TYPE_F32  0
 #define LAPSUM_TYPE_F16  1
