@@ -32,3 +32,20 @@ def test_select_about_zero(R, n, k, kind):
     idx, w = R.select(torch.from_numpy(r).cuda(), k, p)
     assert np.array_equal(idx.cpu().numpy(), ref.select(r, k))
     assert torch.equal(w, p.gather(1, idx.long()))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("-inf"), float("inf"), -0.0, -2.0 ** -149, -3.4028235e38])
+@pytest.mark.parametrize("n,ks", [(1, [1]), (50, [1, 9, 50]), (1000, [3, 500]), (1500, [9, 700]), (6000, [30, 6000]),
+                                  (16_000, [100, 5000]), (20_000, [150, 15_000]), (40_000, [1, 30, 20_000, 40_000])])
+def test_select_rows_of_one_value(R, n, ks, value):
+    # a row that a mask leaves empty, one that it leaves a score or a few, and an ordinary one
+    g = np.random.default_rng(n)
+    r = np.full((4, n), value, np.float32)
+    r[1, g.integers(0, n)] = 1.0
+    r[2, g.integers(0, n, 1 + n // 100)] = 1.0
+    r[3] = g.standard_normal(n)
+    p = torch.rand(4, n, device="cuda")
+    for k in ks:
+        idx, w = R.select(torch.from_numpy(r).cuda(), k, p)
+        assert np.array_equal(idx.cpu().numpy(), ref.select(r, k)), k
+        assert torch.equal(w, p.gather(1, idx.long()))

@@ -250,3 +250,13 @@ def test_the_restated_passes_on_ordinary_rows(keys):
             seen |= route
             assert bad == 0 and np.array_equal(idx, ref.select(r32[None], k)[0]), k
     assert seen & 4
+
+
+@pytest.mark.parametrize("value", [np.nan, -np.inf, np.inf, -0.0, -2.0 ** -149, -3.4028235e38])
+@pytest.mark.parametrize("others", [0, 1, 40])
+def test_long_rows_of_one_value(keys, value, others):
+    r = np.full(40_000, value, np.float32)
+    r[np.random.default_rng(1).integers(0, r.size, others)] = 1.0
+    for k in (1, 30, 20_000, 40_000):
+        bad, idx, _ = long_row(keys, r, k)
+        assert bad == 0 and np.array_equal(idx, ref.select(r[None], k)[0]), k
