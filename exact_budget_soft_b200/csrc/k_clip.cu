@@ -4,9 +4,9 @@
 //
 // Two launches per group of up to CLIP_GROUP tensors: the first leaves one fp64
 // partial sum a block, the second adds the partials up in a fixed order (every
-// block the same sum), forms the scale and writes.  The scale is rounded to fp32, since
-// fp64 products would cost more than the values' bytes; so an output carries its
-// rounding, the product's and its type's.  The tensors' addresses and
+// block the same sum), forms the scale and writes.  The scale is rounded to fp32, half
+// a step of an fp32 output and far below a 16-bit one's: products and values then stay
+// in 32 bits.  An output carries that rounding, the product's and its type's.  The tensors' addresses and
 // sizes travel as kernel parameters: nothing is copied to the device, and a
 // captured graph holds them.  Tensors are cut into chunks of CLIP_VECS 16-byte
 // vectors; a block takes an even share of consecutive chunks, the second launch each
